@@ -14,8 +14,11 @@
 // 256 x 256 tile of C (each CTA's TMEM 128 rows; each CTA's shared memory its own 128 rows of
 // A and half of B), unit by unit:
 //   warp 0      TMA producer (every CTA): a ring of 32 KB stages, one 128-block each, and the
-//               block's column scales where every column of C has its own
+//               block's row scales and, where every column of C has its own, column scales
 //   warp 1      TMEM owner (every CTA); in the even CTA the MMA issuer
+//   warp 2      sees a block's scales land in this CTA and passes that on to the epilogue (every
+//               CTA): a completed MMA says that copies have landed, but makes what they wrote
+//               visible to no thread (the epilogue's own wait for the scales cost 7 %)
 //   warps 4..11 epilogue (every CTA): thread = one row of C, 128 columns in registers (or 4 rows,
 //               32 columns: below)
 // Two 256-column accumulators alternate, so the MMAs of one block overlap the scaling of the
@@ -64,7 +67,7 @@ constexpr int NSCALE = 16;
 constexpr int ROW_SCALE_BYTES = BM * 4;
 constexpr int COL_SCALE_BYTES = BN * 4;
 constexpr int SMEM_BYTES =
-    NSTAGE * STAGE_BYTES + NSCALE * (ROW_SCALE_BYTES + COL_SCALE_BYTES) + 1024 + 256;
+    NSTAGE * STAGE_BYTES + NSCALE * (ROW_SCALE_BYTES + COL_SCALE_BYTES) + 1024 + 384;
 constexpr int PART_LD = BN + 4;  // floats of a row of shared sums
 static_assert(BM * PART_LD * 4 <= NSTAGE * STAGE_BYTES, "the shared sums reuse the ring");
 constexpr int EPI_WARPS = 8;
@@ -98,6 +101,16 @@ __device__ __forceinline__ void decode_unit(int64_t u, const MatmulArgs& a, int6
   const int64_t rows = min(static_cast<int64_t>(kBand), a.mt - band * kBand);
   im = band * kBand + rem % rows;
   in = rem / rows;
+}
+
+// On every exit of a producer: the scales that it asked for have landed (the last of each slot)
+__device__ __forceinline__ bool drain_scales(uint64_t* scaled, int issued) {
+  bool landed = true;
+  for (int k = max(0, issued - NSCALE); k < issued; ++k)
+    if (!tc::mbar_wait_for(&scaled[k % NSCALE], static_cast<uint32_t>(k / NSCALE) & 1u, kWaitLimitNs))
+      landed = false;
+  if (!landed) tc::linger();
+  return landed;
 }
 
 // 32 bytes, a whole sector, in one store (p 32-byte aligned)
@@ -187,17 +200,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                       const __grid_constant__ CUtensorMap tsa,
                       const __grid_constant__ CUtensorMap tsb, const MatmulArgs a) {
   constexpr uint32_t IDESC = tc::idesc_e4m3_f32(2 * BM, BN, false, B_MN);
-  constexpr uint32_t TX_BYTES = STAGE_BYTES + ROW_SCALE_BYTES + (COL ? COL_SCALE_BYTES : 0);  // per CTA and stage
+  constexpr uint32_t SCALE_BYTES = ROW_SCALE_BYTES + (COL ? COL_SCALE_BYTES : 0);  // of a block
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* row_scales = reinterpret_cast<float*>(smem + NSTAGE * STAGE_BYTES);
   float* col_scales = row_scales + NSCALE * BM;
   uint64_t* full = reinterpret_cast<uint64_t*>(col_scales + NSCALE * BN);
-  uint64_t* done = full + NSTAGE;     // a stage's MMAs have completed: its operands may be
-                                      // replaced and its accumulator read
+  uint64_t* done = full + NSTAGE;     // a stage's MMAs have completed and its block's scales are
+                                      // there: its operands may be replaced, its accumulator read
   uint64_t* accempty = done + NSTAGE;
-  uint64_t* mma_drain = accempty + 2;
+  uint64_t* scaled = accempty + 2;    // a block's scales are in their slot of this CTA
+  uint64_t* mma_drain = scaled + NSCALE;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* counts = const_cast<int*>(abort_flag) + 1;  // [0] stages issued here, [1] stages seen to land
@@ -216,11 +230,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NSTAGE; ++s) {
       tc::mbar_init(&full[s], 1);
-      tc::mbar_init(&done[s], 1);
+      tc::mbar_init(&done[s], 2);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&accempty[b], 2 * EPI_WARPS);
     }
+    for (int s = 0; s < NSCALE; ++s) tc::mbar_init(&scaled[s], 1);
     tc::mbar_init(mma_drain, 1);
     *abort_flag = 0;
     counts[0] = counts[1] = 0;
@@ -374,18 +389,20 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (!tc::mbar_wait_short(&done[stage], phase ^ 1u, abort_flag, a.wait_ns)) { ok = false; break; }
           uint8_t* sa = smem + stage * STAGE_BYTES;
           const uint32_t bar = tc::mapa_shared(tc::smem_u32(&full[stage]), lead);
-          if (crank == 0) tc::mbar_arrive_expect_tx(&full[stage], 2 * TX_BYTES);
+          if (crank == 0) tc::mbar_arrive_expect_tx(&full[stage], 2 * STAGE_BYTES);
           tc::tma_load_2d_pair(sa, &ta, bar, kb * BK, row);
           if (B_MN) tc::tma_load_2d_pair(sa + A_BYTES, &tb, bar, col, kb * BK);
           else tc::tma_load_2d_pair(sa + A_BYTES, &tb, bar, kb * BK, col);
-          tc::tma_load_2d_pair(row_scales + (issued % NSCALE) * BM, &tsa, bar, row, kb);
-          if (COL)
-            tc::tma_load_2d_pair(col_scales + (issued % NSCALE) * BN, &tsb, bar, static_cast<int>(in * BN), kb);
+          const int slot = issued % NSCALE;
+          tc::mbar_arrive_expect_tx(&scaled[slot], SCALE_BYTES);
+          tc::tma_load_2d(row_scales + slot * BM, &tsa, &scaled[slot], row, kb);
+          if (COL) tc::tma_load_2d(col_scales + slot * BN, &tsb, &scaled[slot], static_cast<int>(in * BN), kb);
           ++issued;
           if (++stage == NSTAGE) { stage = 0; phase ^= 1u; }
         }
       }
       counts[0] = issued;
+      if (!drain_scales(scaled, issued)) ok = false;
     } else if (crank == 0 && warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
       const uint32_t ring = tc::smem_u32(smem);
@@ -418,6 +435,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (lane == 0) counts[1] = seen;
+    } else if (warp == 2 && lane == 0) {
+      // ---------------------------------------------------------------- the scales' landing
+      int i = 0;  // the producer fills a slot again only behind `done` of six blocks before
+      for (int64_t u = unit0; u < units && ok; u += unit_step) {
+        for (int kb = 0; kb < nb; ++kb, ++i) {
+          if (!tc::mbar_wait(&scaled[i % NSCALE], static_cast<uint32_t>(i / NSCALE) & 1u, abort_flag, a.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc::mbar_arrive(&done[i % NSTAGE]);
+        }
+      }
     }
   }
   griddep_launch_dependents();
@@ -429,7 +458,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       atomicAdd(&a.st->timeouts, 1);
     }
   }
-  // Drain on every exit: the MMAs by one more commit, then every copy that was issued.
+  // Drain on every exit: the MMAs by one more commit, then every operand copy that was issued.
   bool drained = true;
   if (crank == 0 && warp == 1 && tc::elect_one()) {  // the lane that issued the MMAs
     tc::mma_commit_pair(mma_drain, static_cast<uint16_t>(0x1u << lead));
@@ -440,14 +469,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc::cluster_sync();  // both producers have stopped; their counts are visible
   if (crank == 0 && threadIdx.x == 0) {
     const int other = static_cast<int>(tc::ld_shared_cluster_u32(tc::mapa_shared(tc::smem_u32(counts), lead + 1)));
-    if (!tc::drain_pair_stages(full, NSTAGE, counts[1], counts[0], other, TX_BYTES)) drained = false;
+    if (!tc::drain_pair_stages(full, NSTAGE, counts[1], counts[0], other, STAGE_BYTES)) drained = false;
   }
   if (!drained) {
     dev_fail(a.st, GPTQ_ERR_TIMEOUT, 1);
     atomicAdd(&a.st->timeouts, 1);
-    const uint64_t t0 = global_ns();
-    while (global_ns() - t0 < 200000ull) {
-    }
+    tc::linger();
   }
   if constexpr (SPLIT) {
     // every CTA joins its share of its 128 rows, over the pairs in order

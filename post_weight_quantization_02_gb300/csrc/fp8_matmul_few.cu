@@ -108,12 +108,13 @@ __global__ void __launch_bounds__(THREADS + (std::is_void_v<TX> ? 0 : 32 * QUANT
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* xscales = reinterpret_cast<float*>(smem + NSTAGE * STAGE_BYTES);
   uint64_t* full = reinterpret_cast<uint64_t*>(xscales + NSCALE * F::SLOT);
-  uint64_t* done = full + NSTAGE;     // a stage's MMAs have completed: its operands may be
-                                      // replaced and its accumulator read
+  // A stage's MMAs have completed: its operands may be replaced and its accumulator read.  The
+  // issuer arrives too: it has seen the block's token scales land, and passes that on to the
+  // epilogue (a completed MMA alone makes what copies or other warps wrote visible to no thread).
+  uint64_t* done = full + NSTAGE;
   uint64_t* accempty = done + NSTAGE;
   uint64_t* mma_drain = accempty + NACC;
-  uint64_t* quantised = mma_drain + 1;  // a block's token scales are in their slot
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(quantised + NSCALE);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // [0] stages issued, [1] stages seen to land, [2 + w] groups that quantiser warp w made
   int* counts = const_cast<int*>(abort_flag) + 1;
@@ -131,10 +132,9 @@ __global__ void __launch_bounds__(THREADS + (std::is_void_v<TX> ? 0 : 32 * QUANT
   if (warp == 0) {  // a barrier a lane
     if (lane < NSTAGE) {
       tc::mbar_init(&full[lane], QUANT ? 1 + QUANT_WARPS : 1);
-      tc::mbar_init(&done[lane], 1);
+      tc::mbar_init(&done[lane], 2);
     }
     if (lane < NACC) tc::mbar_init(&accempty[lane], EPI_WARPS);
-    if (QUANT) tc::mbar_init(&quantised[lane], QUANT_WARPS);
     if (lane == 0) {
       tc::mbar_init(mma_drain, 1);
       *abort_flag = 0;
@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(THREADS + (std::is_void_v<TX> ? 0 : 32 * QUANT
         for (int kk = 0; kk < BK / 32; ++kk)  // N-major: 32 rows of k are four 8-row groups
           tc::mma_f8(d, wd + (W_MN ? 256 : 2) * kk, xd + 2 * kk, IDESC, kk != 0 ? 1u : 0u);
         tc::mma_commit(&done[stage]);
+        tc::mbar_arrive(&done[stage]);
       }
       __syncwarp();
       if (++stage == NSTAGE) { stage = 0; phase ^= 1u; }
@@ -263,10 +264,7 @@ __global__ void __launch_bounds__(THREADS + (std::is_void_v<TX> ? 0 : 32 * QUANT
           tc::fence_proxy_async_shared();  // the tensor core reads what was written
         }
         __syncwarp();
-        if (lane < GROUP && i0 + lane < nb) {
-          tc::mbar_arrive(&full[(i0 + lane) % NSTAGE]);
-          tc::mbar_arrive(&quantised[(i0 + lane) % NSCALE]);
-        }
+        if (lane < GROUP && i0 + lane < nb) tc::mbar_arrive(&full[(i0 + lane) % NSTAGE]);
         ++made;
       }
       if (lane == 0) counts[2 + qw] = made;
@@ -284,8 +282,6 @@ __global__ void __launch_bounds__(THREADS + (std::is_void_v<TX> ? 0 : 32 * QUANT
       }
       const float s = __shfl_sync(0xffffffffu, sw, i % 32);
       if (!tc::mbar_wait_short(&done[stage], phase, abort_flag, a.wait_ns)) { ok = false; break; }
-      if (QUANT && !tc::mbar_wait_short(&quantised[i % NSCALE], static_cast<uint32_t>(i / NSCALE) & 1u,
-                                        abort_flag, a.wait_ns)) { ok = false; break; }
       tc::fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                              static_cast<uint32_t>(acc * NT + half * HALF);
@@ -346,9 +342,7 @@ __global__ void __launch_bounds__(THREADS + (std::is_void_v<TX> ? 0 : 32 * QUANT
   if (!drained) {
     dev_fail(a.st, GPTQ_ERR_TIMEOUT, 1);
     atomicAdd(&a.st->timeouts, 1);
-    const uint64_t w0 = global_ns();
-    while (global_ns() - w0 < 200000ull) {
-    }
+    tc::linger();
   }
   __syncthreads();
   griddep_wait();  // every thread, before C is written: the work before may still read it

@@ -106,6 +106,13 @@ __device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity,
   }
 }
 
+// The last resort of a drain whose wait ran out: 200 us for what is still in flight.
+__device__ __forceinline__ void linger() {
+  const uint64_t t0 = global_ns();
+  while (global_ns() - t0 < 200000ull) {
+  }
+}
+
 // The same wait for a drain at a kernel's exit: no abort flag, only the time limit.
 __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   const uint32_t a = smem_u32(bar);

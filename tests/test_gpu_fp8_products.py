@@ -1,0 +1,61 @@
+"""The 8-bit products where a CTA works on many tiles and blocks."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_fp8 import (BF16, F32, check_product, dequantized, make_layer, np32,
+                                weight_values)
+
+pytestmark = pytest.mark.gpu
+
+
+def varied(rng, r, c, dtype, dev):
+    """Values whose groups of 128, along either axis, differ in size by powers of two."""
+    x = rng.standard_normal((r, c))
+    x *= np.exp2(rng.integers(-6, 7, (r, -(-c // 128))).repeat(128, 1)[:, :c])
+    x *= np.exp2(rng.integers(-6, 7, (-(-r // 128), c)).repeat(128, 0)[:r])
+    return torch.from_numpy(x.astype(np.float32)).to(dtype).to(dev)
+
+
+@pytest.mark.parametrize("t,n,k", [(2500, 2600, 2300),    # 99 tiles, 20 token blocks
+                                   (300, 4200, 2400),     # 170 tiles, 3 blocks
+                                   (4300, 300, 200)])     # 2 tiles, 34 blocks
+@pytest.mark.parametrize("wdt", [F32, BF16])
+def test_weight_gradient_of_many_tiles(lib, cuda_device, t, n, k, wdt):
+    """More tiles than pairs of SMs and more token blocks than scale slots, with scales that
+    differ from block to block and from column to column."""
+    rng = np.random.default_rng(t + n + k)
+    x, dy = varied(rng, t, k, BF16, cuda_device), varied(rng, t, n, BF16, cuda_device)
+    g = torch.Generator().manual_seed(43)
+    codes, scales = make_layer(lib, g, n, k, cuda_device)
+    _, dw = lib.gptq_fp8_linear_backward(dy, x, codes, scales, need_dx=False, dw_dtype=wdt)
+    check_product(dw, dequantized(np32(dy), "columns").T, dequantized(np32(x), "columns"))
+    for _ in range(5):                                # the same bits every time
+        assert torch.equal(lib.gptq_fp8_linear_backward(dy, x, codes, scales, need_dx=False,
+                                                        dw_dtype=wdt)[1], dw)
+    lib.gptq_async_status()
+
+
+# many tiles; 9 x 9 tiles with a shared last wave; shared contractions; few tokens with more
+# blocks a CTA than scale slots; tokens that the product quantises itself
+@pytest.mark.parametrize("t,n,k", [(2600, 4400, 2300), (2300, 2200, 4200), (700, 1100, 5003),
+                                   (12, 300, 40000), (50, 300, 40000), (100, 300, 40000),
+                                   (3, 300, 40000), (8, 1000, 16000)])
+def test_products_with_scales_of_every_size(lib, cuda_device, t, n, k):
+    """Output and input gradient with a scale for each token and block that differs from its
+    neighbours' by powers of two, repeated."""
+    rng = np.random.default_rng(t + n + k)
+    w = varied(rng, n, k, F32, cuda_device) * 2.0 ** -5
+    codes, scales = lib.gptq_fp8_quantize(w)
+    x = varied(rng, t, k, BF16, cuda_device)
+    y = lib.gptq_fp8_linear(x, codes, scales, dtype=F32)
+    check_product(y, dequantized(np32(x), "rows"), weight_values(codes, scales).T)
+    tcodes, tscales = lib.gptq_fp8_quantize(w.t().contiguous())
+    back = lambda: lib.gptq_fp8_linear_backward(x, None, tcodes, tscales, need_dw=False)[0]
+    dx = back()
+    check_product(dx, dequantized(np32(x), "rows"), weight_values(tcodes, tscales))
+    for _ in range(5):
+        assert torch.equal(lib.gptq_fp8_linear(x, codes, scales, dtype=F32), y)
+        assert torch.equal(back(), dx)
+    lib.gptq_async_status()
