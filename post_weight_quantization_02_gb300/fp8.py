@@ -32,7 +32,11 @@ def _matrix(t: torch.Tensor) -> torch.Tensor:
 class _Fp8LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, codes, scales, dtype):
-        ctx.save_for_backward(x, codes, scales)
+        # the weight's gradient needs no codes: they may change before it is taken (the calls ask
+        # for a weight of the layer's shape all the same)
+        need_dx = ctx.needs_input_grad[0]
+        ctx.save_for_backward(x, codes if need_dx else None, scales if need_dx else None)
+        ctx.unread = None if need_dx else (codes, scales)
         ctx.weight_dtype = None if weight is None else weight.dtype
         ctx.x_dtype = x.dtype
         return G.gptq_fp8_linear(x, codes, scales, dtype=dtype)
@@ -41,6 +45,8 @@ class _Fp8LinearFunction(torch.autograd.Function):
     def backward(ctx, dy):
         x, codes, scales = ctx.saved_tensors
         need_dx, need_dw = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        if not need_dx:
+            codes, scales = ctx.unread
         dy = _matrix(dy)
         dx = None
         if need_dx:
@@ -77,7 +83,8 @@ class Fp8Linear:
                                                  layer.g_idx, bits))
 
     def refresh(self) -> None:
-        """The codes of the kept weight, after it changed."""
+        """The codes of the kept weight, after it changed.  An input gradient of an earlier call
+        has to be taken before (it raises afterwards)."""
         if self.weight is None:
             raise ValueError("no weight was kept")
         G.gptq_fp8_quantize(self.weight.detach(), "blocks", self.codes, self.scales)

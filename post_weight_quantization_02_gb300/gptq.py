@@ -475,6 +475,14 @@ def _stream_of(stream, t: torch.Tensor) -> int:
     return _stream(stream)
 
 
+def _wrote(*tensors: Optional[torch.Tensor]) -> None:
+    """Marks tensors that a call has written through their addresses, so that automatic
+    differentiation does not take them for what it saved."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 @functools.lru_cache(maxsize=256)
 def _ws_bytes(op: int, ntok: int, d_out: int, d_in: int) -> int:
     return max(gptq_workspace_size(op, ntok, d_out, d_in), 256)
@@ -516,6 +524,7 @@ def gptq_fp8_quantize(x: torch.Tensor, form: str = "blocks", codes: Optional[tor
     if form not in FP8_FORMS:
         raise ValueError(f"form must be one of {sorted(FP8_FORMS)}")
     px, r, c, ldx = _rows(x, "x")
+    given = codes, scales
     shape = (c, r) if form == "columns" else (r, c)
     sshape = {"rows": (_blocks(c), r), "columns": (_blocks(r), c),
               "blocks": (_blocks(r), _blocks(c))}[form]
@@ -529,6 +538,7 @@ def gptq_fp8_quantize(x: torch.Tensor, form: str = "blocks", codes: Optional[tor
     _check(lib().gptq_fp8_quantize(px, _dtype_code(x), r, c, ldx, FP8_FORMS[form], pc, ldc,
                                    _buf(scales, torch.float32, sshape[0] * sshape[1], "scales"),
                                    _stream_of(stream, x)))
+    _wrote(*given)
     return codes, scales
 
 
@@ -541,6 +551,7 @@ def gptq_fp8_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     pc, ldw, psc, n, d_in = _weight(codes, scales)
     if k != d_in:
         raise ValueError(f"x has {k} columns, the weight {d_in}")
+    given = y
     if y is None:
         y = _empty((t, n), dtype, x.device, stream)
         py, ldy = y.data_ptr(), n
@@ -555,6 +566,7 @@ def gptq_fp8_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     _check(lib().gptq_fp8_linear(px, _dtype_code(x), t, ldx, pc, ldw, psc, n, k, py,
                                  _dtype_code(y), ldy, _ptr(ws), 0 if ws is None else ws.numel(),
                                  _stream_of(stream, x)))
+    _wrote(given)
     return y
 
 
@@ -594,6 +606,7 @@ def gptq_fp8_linear_backward(dy: torch.Tensor, x: Optional[torch.Tensor], codes:
     _check(lib().gptq_fp8_linear_backward(pdy, _dtype_code(dy), lddy, px, xcode, ldx, t, pc, ldw,
                                           psc, n, k, *outs[0][1:], *outs[1][1:], _ptr(ws),
                                           ws.numel(), _stream_of(stream, dy)))
+    _wrote(dx if need_dx else None, dw if need_dw else None)
     return outs[0][0], outs[1][0]
 
 
@@ -604,7 +617,7 @@ def gptq_top_logits(logits: torch.Tensor, k: int, values: Optional[torch.Tensor]
     indices int32 [rows, k], descending, equal values by ascending index, and the rows'
     log-sum-exp float32 [rows].  Only enqueues."""
     pl, n, v, ld = _rows(logits, "logits")
-    k, dev = int(k), logits.device
+    k, dev, given = int(k), logits.device, (values, indices, lse)
     if values is None:
         values = _empty((n, k), torch.float32, dev, stream)
     if indices is None:
@@ -615,6 +628,7 @@ def gptq_top_logits(logits: torch.Tensor, k: int, values: Optional[torch.Tensor]
                                  _buf(values, torch.float32, n * k, "values"),
                                  _buf(indices, torch.int32, n * k, "indices"),
                                  _buf(lse, torch.float32, n, "lse"), _stream_of(stream, logits)))
+    _wrote(*given)
     return values, indices, lse
 
 
@@ -638,6 +652,7 @@ def gptq_distill_loss(logits: torch.Tensor, values: torch.Tensor, indices: torch
     student's logits that gptq_distill_backward needs.  Only enqueues."""
     pl, n, v, ld = _rows(logits, "logits")
     k, pv, pi, pw = _teacher(values, indices, weights, n)
+    given = loss, lse
     if loss is None:
         loss = _empty((n,), torch.float32, logits.device, stream)
     if lse is None:
@@ -645,6 +660,7 @@ def gptq_distill_loss(logits: torch.Tensor, values: torch.Tensor, indices: torch
     _check(lib().gptq_distill_loss(pl, _dtype_code(logits), n, v, ld, pv, pi, k,
                                    float(temperature), pw, _buf(loss, torch.float32, n, "loss"),
                                    _buf(lse, torch.float32, n, "lse"), _stream_of(stream, logits)))
+    _wrote(*given)
     return loss, lse
 
 
@@ -666,12 +682,14 @@ def gptq_distill_backward(logits: torch.Tensor, lse: torch.Tensor, values: torch
     losses; ``dlogits`` may be the logits themselves.  Only enqueues."""
     pl, n, v, ld = _rows(logits, "logits")
     k, pv, pi, pw = _teacher(values, indices, weights, n)
+    given = dlogits
     dlogits, pd, ldd = _gradient(logits, dlogits, stream)
     _check(lib().gptq_distill_backward(pl, _dtype_code(logits), n, v, ld,
                                        _buf(lse, torch.float32, n, "lse"), pv, pi, k,
                                        float(temperature), pw,
                                        _buf(grad_loss, torch.float32, n, "grad_loss"), pd, ldd,
                                        _stream_of(stream, logits)))
+    _wrote(given)
     return dlogits
 
 
@@ -683,6 +701,7 @@ def gptq_distill_loss_grad(logits: torch.Tensor, values: torch.Tensor, indices: 
     ``dlogits`` may be the logits themselves.  Only enqueues."""
     pl, n, v, ld = _rows(logits, "logits")
     k, pv, pi, pw = _teacher(values, indices, weights, n)
+    given = loss, dlogits
     if loss is None:
         loss = _empty((n,), torch.float32, logits.device, stream)
     dlogits, pd, ldd = _gradient(logits, dlogits, stream)
@@ -690,6 +709,7 @@ def gptq_distill_loss_grad(logits: torch.Tensor, values: torch.Tensor, indices: 
                                         float(temperature), pw,
                                         _buf(loss, torch.float32, n, "loss"), pd, ldd,
                                         _stream_of(stream, logits)))
+    _wrote(*given)
     return loss, dlogits
 
 
