@@ -33,12 +33,13 @@ class _Fp8LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, codes, scales, dtype):
         # the weight's gradient needs no codes: they may change before it is taken (the calls ask
-        # for a weight of the layer's shape all the same)
-        need_dx = ctx.needs_input_grad[0]
-        ctx.save_for_backward(x, codes if need_dx else None, scales if need_dx else None)
+        # for a weight of the layer's shape all the same); the input's needs no activations
+        need_dx, need_dw = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        ctx.save_for_backward(x if need_dw else None, codes if need_dx else None,
+                              scales if need_dx else None)
         ctx.unread = None if need_dx else (codes, scales)
         ctx.weight_dtype = None if weight is None else weight.dtype
-        ctx.x_dtype = x.dtype
+        ctx.x_shape, ctx.x_dtype = x.shape, x.dtype
         return G.gptq_fp8_linear(x, codes, scales, dtype=dtype)
 
     @staticmethod
@@ -50,8 +51,8 @@ class _Fp8LinearFunction(torch.autograd.Function):
         dy = _matrix(dy)
         dx = None
         if need_dx:
-            dx = torch.empty(x.shape, dtype=ctx.x_dtype, device=x.device)
-        dx, dw = G.gptq_fp8_linear_backward(dy, x if need_dw else None, codes, scales,
+            dx = torch.empty(ctx.x_shape, dtype=ctx.x_dtype, device=dy.device)
+        dx, dw = G.gptq_fp8_linear_backward(dy, x, codes, scales,
                                             need_dx=need_dx, need_dw=need_dw, dx=dx,
                                             dw_dtype=ctx.weight_dtype or torch.float32)
         return dx, dw, None, None, None

@@ -93,3 +93,21 @@ def test_written_tensors_are_marked(lib, cuda_device):
         assert all(v._version > before[k] for k, v in outs.items()), outs.keys()
     with torch.inference_mode():                    # tensors without a version
         lib.gptq_fp8_linear(x, codes, scales, y=e(40, 200))
+
+
+def test_what_is_saved(lib, cuda_device):
+    """Activations are kept for the weight's gradient only, codes for the input's only."""
+    def kept(x, layer):
+        seen = []
+        def pack(t):
+            seen.append(t.data_ptr())
+            return t
+        with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+            layer(x)
+        return x.data_ptr() in seen, layer.codes.data_ptr() in seen
+    x = randn(4, 9, 260, device=cuda_device)
+    frozen, trained = make_layer(cuda_device, False)[1], make_layer(cuda_device)[1]
+    assert kept(x, trained) == (True, False)
+    x.requires_grad_()
+    assert kept(x, frozen) == (False, True)
+    assert kept(x, trained) == (True, True)
