@@ -16,7 +16,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import gptq as G
-from .fp8 import Fp8Linear, _matrix
+from .fp8 import Fp8Linear, _matrix, _once
 
 __all__ = ["TopLogits", "top_logits", "distill_loss", "DistilledHead"]
 
@@ -48,7 +48,7 @@ class _DistillFunction(torch.autograd.Function):
         logits, lse, values, indices, weights = ctx.saved_tensors
         d = G.gptq_distill_backward(logits, lse, values, indices, grad_loss.float().contiguous(),
                                     ctx.temperature, weights)
-        return d, None, None, None, None
+        return _once(d, logits, grad_loss), None, None, None, None
 
 
 def distill_loss(logits: torch.Tensor, teacher: TopLogits, temperature: float = 1.0,

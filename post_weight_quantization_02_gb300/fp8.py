@@ -29,6 +29,26 @@ def _matrix(t: torch.Tensor) -> torch.Tensor:
     return t
 
 
+class _Gradient(torch.autograd.Function):
+    """A gradient that a call computed, tied to what it has a derivative in, which is not
+    computed: taking it is an error."""
+
+    @staticmethod
+    def forward(ctx, gradient, *inputs):
+        return gradient
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the 8-bit layer and the distillation loss have no second derivative")
+
+
+def _once(gradient: Optional[torch.Tensor], *inputs: Optional[torch.Tensor]):
+    """What a backward pass returns: under create_graph, where it is recorded, not a constant."""
+    if gradient is None or not torch.is_grad_enabled():
+        return gradient
+    return _Gradient.apply(gradient, *inputs)
+
+
 class _Fp8LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, codes, scales, dtype):
@@ -38,6 +58,7 @@ class _Fp8LinearFunction(torch.autograd.Function):
         ctx.save_for_backward(x if need_dw else None, codes if need_dx else None,
                               scales if need_dx else None)
         ctx.unread = None if need_dx else (codes, scales)
+        ctx.weight = weight
         ctx.weight_dtype = None if weight is None else weight.dtype
         ctx.x_shape, ctx.x_dtype = x.shape, x.dtype
         return G.gptq_fp8_linear(x, codes, scales, dtype=dtype)
@@ -46,16 +67,16 @@ class _Fp8LinearFunction(torch.autograd.Function):
     def backward(ctx, dy):
         x, codes, scales = ctx.saved_tensors
         need_dx, need_dw = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
-        if not need_dx:
+        if codes is None:
             codes, scales = ctx.unread
-        dy = _matrix(dy)
+        upstream, dy = dy, _matrix(dy)
         dx = None
         if need_dx:
             dx = torch.empty(ctx.x_shape, dtype=ctx.x_dtype, device=dy.device)
         dx, dw = G.gptq_fp8_linear_backward(dy, x, codes, scales,
                                             need_dx=need_dx, need_dw=need_dw, dx=dx,
                                             dw_dtype=ctx.weight_dtype or torch.float32)
-        return dx, dw, None, None, None
+        return _once(dx, upstream, ctx.weight), _once(dw, upstream, x), None, None, None
 
 
 class Fp8Linear:

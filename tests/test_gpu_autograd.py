@@ -1,5 +1,6 @@
 """Automatic differentiation of the 8-bit layer and of the distillation loss where the plain answer
-would be a wrong one, as what was saved has been written to.  It is an error."""
+would be a wrong one: what was saved has been written to, or a second derivative is taken.  Each is
+an error."""
 
 import pytest
 import torch
@@ -111,3 +112,21 @@ def test_what_is_saved(lib, cuda_device):
     x.requires_grad_()
     assert kept(x, frozen) == (False, True)
     assert kept(x, trained) == (True, True)
+
+
+# ------------------------------------------------------------------ derivatives that do not exist
+
+def test_second_derivatives(lib, cuda_device):
+    """A gradient taken for a second derivative is the gradient, and differentiating it an error,
+    also where only the weight or the saved input would have a second-order term."""
+    w, layer = make_layer(cuda_device)
+    x = randn(4, 9, 260, device=cuda_device).requires_grad_()
+    logits, teacher = make_loss(cuda_device)
+    logits.requires_grad_()
+    for out, inp in ((lambda: layer(x).square().sum(), x), (lambda: layer(x).sum(), x),
+                     (lambda: layer(x).sum(), w), (lambda: distill_loss(logits, teacher).sum(), logits)):
+        (ref,) = torch.autograd.grad(out(), (inp,))
+        (grad,) = torch.autograd.grad(out(), (inp,), create_graph=True)
+        assert torch.equal(grad, ref)
+        with pytest.raises(RuntimeError, match="second derivative"):
+            (inp.sum() + grad.square().sum()).backward()
