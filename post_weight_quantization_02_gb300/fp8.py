@@ -13,6 +13,7 @@ from __future__ import annotations
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import gptq as G
 from .api import QuantizedLayer
@@ -27,6 +28,13 @@ def _matrix(t: torch.Tensor) -> torch.Tensor:
     if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
         t = t.contiguous()
     return t
+
+
+def _differentiated(t: Optional[torch.Tensor]) -> bool:
+    """Whether t takes part in automatic differentiation, of either mode (a call that has no
+    forward mode has to say so)."""
+    return t is not None and ((torch.is_grad_enabled() and t.requires_grad)
+                              or unpack_dual(t).tangent is not None)
 
 
 class _Gradient(torch.autograd.Function):
@@ -115,9 +123,7 @@ class Fp8Linear:
         """``x`` [..., d_in] (bf16 or fp32) to [..., d_out] in ``dtype`` (x's by default)."""
         flat = _matrix(x)
         dtype = dtype or x.dtype
-        grad = torch.is_grad_enabled() and (
-            x.requires_grad or (self.weight is not None and self.weight.requires_grad))
-        if grad:
+        if _differentiated(x) or _differentiated(self.weight):
             y = _Fp8LinearFunction.apply(flat, self.weight, self.codes, self.scales, dtype)
         else:
             y = G.gptq_fp8_linear(flat, self.codes, self.scales, dtype=dtype)

@@ -1,11 +1,12 @@
 """Automatic differentiation of the 8-bit layer and of the distillation loss where the plain answer
-would be a wrong one: what was saved has been written to, or a second derivative is taken.  Each is
+would be a wrong one: what was saved has been written to, a second derivative, a tangent.  Each is
 an error."""
 
 import pytest
 import torch
+import torch.autograd.forward_ad as fwd
 
-from post_weight_quantization_02_gb300 import Fp8Linear, distill_loss, top_logits
+from post_weight_quantization_02_gb300 import DistilledHead, Fp8Linear, distill_loss, top_logits
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +131,19 @@ def test_second_derivatives(lib, cuda_device):
         assert torch.equal(grad, ref)
         with pytest.raises(RuntimeError, match="second derivative"):
             (inp.sum() + grad.square().sum()).backward()
+
+
+def test_tangents(lib, cuda_device):
+    w, layer = make_layer(cuda_device, False)
+    x = randn(4, 9, 260, device=cuda_device)
+    logits, teacher = make_loss(cuda_device)
+    with fwd.dual_level():
+        dual = fwd.make_dual(x, torch.ones_like(x))
+        calls = [lambda: layer(dual), lambda: DistilledHead(w).logits(dual),
+                 lambda: distill_loss(fwd.make_dual(logits, torch.ones_like(logits)), teacher)]
+        layer_w = Fp8Linear(layer.codes, layer.scales, fwd.make_dual(w, torch.ones_like(w)))
+        calls.append(lambda: layer_w(x))
+        for call in calls:
+            with pytest.raises(NotImplementedError, match="jvp"):
+                call()
+        layer(x)                                    # nothing here has a tangent
