@@ -53,8 +53,11 @@ class _DistillFunction(torch.autograd.Function):
 
 def distill_loss(logits: torch.Tensor, teacher: TopLogits, temperature: float = 1.0,
                  weights: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Each position's loss, float32 [n], differentiable in ``logits`` [..., vocab]; ``weights``
-    float32 [n] multiply it, and a position of weight 0 does not count."""
+    """Each position's loss, float32 [n], differentiable in ``logits`` [..., vocab] alone;
+    ``weights`` float32 [n] multiply it, and a position of weight 0 does not count."""
+    for t, name in ((weights, "weights"), (teacher.values, "the teacher's values")):
+        if torch.is_grad_enabled() and t is not None and t.requires_grad:
+            raise ValueError(f"{name}: the loss has no gradient in them (detach them)")
     return _DistillFunction.apply(_matrix(logits), teacher.values, teacher.indices,
                                   float(temperature), weights)
 

@@ -1,12 +1,12 @@
 """Automatic differentiation of the 8-bit layer and of the distillation loss where the plain answer
-would be a wrong one: what was saved has been written to, a second derivative, a tangent.  Each is
-an error."""
+would be a wrong one: what was saved has been written to, a second derivative, a tangent, a gradient
+that is not computed.  Each is an error."""
 
 import pytest
 import torch
 import torch.autograd.forward_ad as fwd
 
-from post_weight_quantization_02_gb300 import DistilledHead, Fp8Linear, distill_loss, top_logits
+from post_weight_quantization_02_gb300 import DistilledHead, Fp8Linear, TopLogits, distill_loss, top_logits
 
 pytestmark = pytest.mark.gpu
 
@@ -147,3 +147,20 @@ def test_tangents(lib, cuda_device):
             with pytest.raises(NotImplementedError, match="jvp"):
                 call()
         layer(x)                                    # nothing here has a tangent
+
+
+def test_gradients_of_weights_and_teacher(lib, cuda_device):
+    """The loss has a gradient for the student's logits alone; asking for another is refused."""
+    logits, teacher = make_loss(cuda_device)
+    logits.requires_grad_()
+    w = torch.rand(6, device=cuda_device)
+    ref = distill_loss(logits, teacher, 1.0, w)
+    w.requires_grad_()
+    with pytest.raises(ValueError, match="weights"):
+        distill_loss(logits, teacher, 1.0, w)
+    values = TopLogits(teacher.values.clone().requires_grad_(), teacher.indices, teacher.lse)
+    with pytest.raises(ValueError, match="teacher"):
+        distill_loss(logits, values)
+    assert torch.equal(distill_loss(logits, teacher, 1.0, w.detach()), ref)
+    with torch.no_grad():
+        assert torch.equal(distill_loss(logits, values, 1.0, w), ref)
