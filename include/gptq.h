@@ -27,7 +27,7 @@
  *   the caller's workspace `ws` of `ws_bytes` bytes (size it with gptq_workspace_size; the
  *   base must be 256-byte aligned).  The exceptions are the fixed static array behind
  *   gptq_hessian_accumulate_noalloc (16 MiB + 256 B per GPU that loads the library) and the
- *   256-byte status word that gptq_async_status reads.
+ *   two 256-byte status words behind gptq_async_status.
  *   Host pointers are named as such below.
  * - `stream` is a cudaStream_t passed as void* (NULL = the legacy default stream).  Every
  *   call enqueues its kernels on `stream`, then synchronises `stream` and returns the
@@ -568,11 +568,13 @@ gptq_status gptq_distill_loss_grad(const void* logits, int dtype, int64_t rows, 
                                    float* loss, void* dlogits, int64_t ldd, void* stream);
 
 /*
- * gptq_async_status -- waits for `stream` and reports the first device-side failure since
- * the last report of the calls that only enqueue (gptq_fp8_*, gptq_top_logits,
- * gptq_distill_*) on the current device: TIMEOUT where a device wait ran out (the outputs are
- * unset), INVALID_ARG where a teacher index was out of range.  The status is shared by all
- * streams of the device.  Errors: those, CUDA.
+ * gptq_async_status -- waits for `stream` and reports the device-side failures since the
+ * last report of the calls that only enqueue (gptq_fp8_*, gptq_top_logits, gptq_distill_*)
+ * on the current device: TIMEOUT where a device wait ran out (the outputs are unset), also
+ * where there was an index out of range too; INVALID_ARG, with the first of them, where only
+ * teacher indices were out of range.  The status is shared by all streams of the device, and
+ * taken and cleared at once: a failure on another stream is in this report or in the next.
+ * Errors: those, CUDA.
  */
 gptq_status gptq_async_status(void* stream);
 

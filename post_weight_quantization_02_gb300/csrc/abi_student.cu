@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstring>
 #include <limits>
+#include <mutex>
 
 #include "abi_common.cuh"
 #include "common.cuh"
@@ -17,6 +18,15 @@ namespace gptq {
 namespace {
 
 __device__ __align__(256) DevStatus g_async_status;  // zero when the module loads
+__device__ __align__(256) DevStatus g_async_taken;   // what a report took of it
+
+// Takes the status and clears it in one go: a failure that another stream's kernel records
+// meanwhile is in this report or in the next.
+__global__ void take_status_kernel() {
+  g_async_taken.timeouts = atomicExch(&g_async_status.timeouts, 0);
+  g_async_taken.code = atomicExch(&g_async_status.code, 0);
+  g_async_taken.info = g_async_status.info;
+}
 
 // Address of the status word on the current device, asked from the runtime once per host
 // thread and device.
@@ -378,17 +388,21 @@ gptq_status gptq_distill_loss_grad(const void* logits, int dtype, int64_t rows, 
 gptq_status gptq_async_status(void* stream) {
   return guarded([&] {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    DevStatus* st = async_status();
     DevStatus h;
     std::memset(&h, 0, sizeof(h));
-    GPTQ_CUDA(cudaMemcpyAsync(&h, st, 3 * sizeof(int), cudaMemcpyDeviceToHost, s));
-    GPTQ_CUDA(cudaStreamSynchronize(s));
+    {
+      static std::mutex mu;  // of g_async_taken
+      std::lock_guard<std::mutex> lock(mu);
+      take_status_kernel<<<1, 1, 0, s>>>();
+      GPTQ_CUDA(cudaGetLastError());
+      GPTQ_CUDA(cudaMemcpyFromSymbolAsync(&h, g_async_taken, 3 * sizeof(int), 0, cudaMemcpyDeviceToHost, s));
+      GPTQ_CUDA(cudaStreamSynchronize(s));
+    }
     trace_flush();
-    if (h.code == 0) return;
-    GPTQ_CUDA(cudaMemsetAsync(st, 0, sizeof(DevStatus), s));
-    GPTQ_CUDA(cudaStreamSynchronize(s));
-    if (h.code == GPTQ_ERR_TIMEOUT)
+    // a wait that ran out leaves outputs unset: it comes before whatever else was recorded
+    if (h.timeouts != 0 || h.code == GPTQ_ERR_TIMEOUT)
       fail(GPTQ_ERR_TIMEOUT, "%d device-side wait(s) of an enqueued call ran out", h.timeouts);
+    if (h.code == 0) return;
     if (h.code == GPTQ_ERR_INVALID_ARG)
       fail(GPTQ_ERR_INVALID_ARG, "a teacher index (%d) is not below the vocabulary's size", h.info);
     fail(static_cast<gptq_status>(h.code), "an enqueued call reported status %d", h.code);

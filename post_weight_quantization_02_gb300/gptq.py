@@ -714,8 +714,9 @@ def gptq_distill_loss_grad(logits: torch.Tensor, values: torch.Tensor, indices: 
 
 
 def gptq_async_status(stream=None) -> None:
-    """Wait for the stream; raise the first device-side failure of the calls that only enqueue
-    (gptq_fp8_*, gptq_top_logits, gptq_distill_*) since the last report."""
+    """Wait for the stream; raise the device-side failure of the calls that only enqueue
+    (gptq_fp8_*, gptq_top_logits, gptq_distill_*) since the last report (a wait that ran out
+    before a teacher index out of range)."""
     _check(lib().gptq_async_status(_stream(stream)))
 
 

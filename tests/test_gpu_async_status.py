@@ -1,0 +1,54 @@
+"""What the calls that only enqueue report afterwards."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def setup(lib, dev):
+    g = torch.Generator(device=dev).manual_seed(0)
+    x = torch.randn(200, 1024, generator=g, device=dev)
+    codes, scales = lib.gptq_fp8_quantize(torch.randn(512, 1024, generator=g, device=dev))
+    logits = torch.randn(4, 900, generator=g, device=dev)
+    tv = torch.zeros(4, 8, device=dev)
+    ti = torch.arange(32, dtype=torch.int32, device=dev).reshape(4, 8)
+    bad = ti.clone()
+    bad[1, 4] = 900
+    linear = lambda **kw: lib.gptq_fp8_linear(x, codes, scales, **kw)
+    return linear, lambda i=ti: lib.gptq_distill_loss(logits, tv, i), bad
+
+
+def report(lib):
+    with pytest.raises(lib.GptqError) as e:
+        lib.gptq_async_status()
+    return e.value.status
+
+
+@pytest.mark.parametrize("index_first", [True, False])
+def test_a_timeout_is_always_reported(lib, cuda_device, index_first):
+    """Outputs are unset after a wait that ran out, but right after a bad index: the index must not
+    hide the wait."""
+    linear, distill, bad = setup(lib, cuda_device)
+    linear(), distill()
+    lib.gptq_async_status()
+    try:
+        if index_first:
+            distill(bad)
+            torch.cuda.synchronize()
+        lib.gptq_set_wait_limit(1)
+        linear()
+        lib.gptq_set_wait_limit(0)
+        if not index_first:
+            torch.cuda.synchronize()
+            distill(bad)
+        assert report(lib) == lib.GPTQ_ERR_TIMEOUT
+    finally:
+        lib.gptq_set_wait_limit(0)
+    lib.gptq_async_status()                         # once
+    distill(bad)
+    assert report(lib) == lib.GPTQ_ERR_INVALID_ARG
+    lib.gptq_async_status()
+    ref = linear()
+    assert torch.equal(linear(), ref)
+    lib.gptq_async_status()
