@@ -90,6 +90,8 @@ void trace_end(int kind, cudaStream_t s) {
   cuda_check(cudaEventRecord(p.stop, s), "cudaEventRecord");
 }
 
+// The launches of calls that only enqueue may be on a stream that was not waited for: those that
+// have not ended stay pending.
 void trace_flush() {
   if (t_pending.empty()) return;
   std::vector<Pending> done;
@@ -97,10 +99,18 @@ void trace_flush() {
   std::lock_guard<std::mutex> lk(g_mu);
   for (const Pending& p : done) {
     float ms = 0.f;
-    if (p.stop != nullptr && cudaEventElapsedTime(&ms, p.start, p.stop) == cudaSuccess &&
-        p.kind >= 0 && p.kind < GPTQ_K_COUNT) {
-      g_ms[p.kind] += ms;
-      g_count[p.kind] += 1;
+    cudaError_t e = p.stop != nullptr ? cudaEventQuery(p.stop) : cudaSuccess;
+    if (e == cudaSuccess && p.stop != nullptr && p.kind >= 0 && p.kind < GPTQ_K_COUNT) {
+      e = cudaEventElapsedTime(&ms, p.start, p.stop);
+      if (e == cudaSuccess) {
+        g_ms[p.kind] += ms;
+        g_count[p.kind] += 1;
+      }
+    }
+    if (e != cudaSuccess) cudaGetLastError();  // it is no error of the next launch
+    if (e == cudaErrorNotReady) {
+      t_pending.push_back(p);
+      continue;
     }
     t_pool.push_back(p.start);
     if (p.stop != nullptr) t_pool.push_back(p.stop);

@@ -1,9 +1,11 @@
-"""What the calls that only enqueue report afterwards."""
+"""What the calls that only enqueue report afterwards: failures and traced times."""
 
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
+
+QUANTIZE, MATMUL, DISTILL = 24, 25, 27        # gptq_kernel_kind values
 
 
 def setup(lib, dev):
@@ -52,3 +54,36 @@ def test_a_timeout_is_always_reported(lib, cuda_device, index_first):
     ref = linear()
     assert torch.equal(linear(), ref)
     lib.gptq_async_status()
+
+
+@pytest.fixture
+def tracing(lib):
+    lib.gptq_profile_enable(True)
+    lib.gptq_profile_reset()
+    yield
+    lib.gptq_profile_enable(False)
+    lib.gptq_profile_reset()
+
+
+def test_trace_of_another_stream(lib, cuda_device, tracing):
+    """Waiting for one stream collects the times of launches that have ended; those of another
+    stream that have not are collected when they have, and disturb no call between."""
+    linear, distill, _ = setup(lib, cuda_device)
+    linear(), distill()
+    lib.gptq_async_status()
+    lib.gptq_profile_reset()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)              # about a tenth of a second
+    linear(stream=side)
+    distill()
+    lib.gptq_async_status()                         # the current stream's alone
+    assert not side.query()
+    assert lib.gptq_profile_read(DISTILL)[1] == 1 and lib.gptq_profile_read(MATMUL)[1] == 0
+    distill()
+    lib.gptq_async_status()
+    lib.gptq_async_status(stream=side)
+    assert lib.gptq_profile_read(DISTILL)[1] == 2
+    ms, n = lib.gptq_profile_read(MATMUL)
+    assert n == 1 and 0 < ms < 50
+    assert lib.gptq_profile_read(QUANTIZE)[1] == 1
