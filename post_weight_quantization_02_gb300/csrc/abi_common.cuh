@@ -11,20 +11,21 @@ namespace gptq {
 // Runs an entry point's body; no C++ exception leaves it.
 template <typename F>
 gptq_status guarded(F&& f) {
+  const size_t mark = trace_mark();
   try {
     f();
     set_last_error("");
     return GPTQ_OK;
   } catch (const Error& e) {
-    trace_discard();
+    trace_discard(mark);
     set_last_error(e.msg);
     return e.status;
   } catch (const std::exception& e) {
-    trace_discard();
+    trace_discard(mark);
     set_last_error(std::string("internal error: ") + e.what());
     return GPTQ_ERR_CUDA;
   } catch (...) {
-    trace_discard();
+    trace_discard(mark);
     set_last_error("internal error");
     return GPTQ_ERR_CUDA;
   }

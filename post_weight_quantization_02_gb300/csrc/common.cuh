@@ -97,7 +97,8 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 void trace_begin(int kind, cudaStream_t s);
 void trace_end(int kind, cudaStream_t s);
 void trace_flush();    // after the call's stream is synchronised
-void trace_discard();  // on failure: drop this thread's pending events
+size_t trace_mark();    // how many launches of this thread are pending
+void trace_discard(size_t mark);  // on failure: drop those since the mark
 void profile_enable(bool on);
 void profile_select(uint32_t mask);
 void profile_reset();

@@ -117,12 +117,14 @@ void trace_flush() {
   }
 }
 
-void trace_discard() {
-  for (const Pending& p : t_pending) {
+// The launches of earlier calls that only enqueued are not the failed call's.
+size_t trace_mark() { return t_pending.size(); }
+void trace_discard(size_t mark) {
+  for (; t_pending.size() > mark; t_pending.pop_back()) {
+    const Pending& p = t_pending.back();
     t_pool.push_back(p.start);
     if (p.stop != nullptr) t_pool.push_back(p.stop);
   }
-  t_pending.clear();
 }
 
 void profile_enable(bool on) { g_enabled.store(on); }

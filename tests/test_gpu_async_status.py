@@ -87,3 +87,15 @@ def test_trace_of_another_stream(lib, cuda_device, tracing):
     ms, n = lib.gptq_profile_read(MATMUL)
     assert n == 1 and 0 < ms < 50
     assert lib.gptq_profile_read(QUANTIZE)[1] == 1
+
+
+def test_trace_survives_a_refused_call(lib, cuda_device, tracing):
+    _, distill, _ = setup(lib, cuda_device)
+    distill()
+    lib.gptq_async_status()
+    lib.gptq_profile_reset()
+    distill()
+    with pytest.raises(lib.GptqError):
+        lib.gptq_top_logits(torch.zeros(2, 300, device=cuda_device), 257)
+    lib.gptq_async_status()
+    assert lib.gptq_profile_read(DISTILL)[1] == 1
