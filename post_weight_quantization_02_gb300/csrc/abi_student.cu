@@ -75,6 +75,12 @@ void plan_operand(WsPlan& w, int64_t rows, int64_t cols) {
   w.add<float>(static_cast<size_t>(ceil_div(cols, 128)) * scale_ld(rows));
 }
 
+// pointers to 32-bit numbers, null or not
+template <typename... P>
+void check_words(const char* msg, const P*... p) {
+  require((aligned(p, 4) && ...), GPTQ_ERR_INVALID_ARG, msg);
+}
+
 void check_logits(const void* logits, int dtype, int64_t rows, int32_t vocab, int64_t ld,
                   int32_t k) {
   require(rows >= 0 && vocab > 0 && ld >= vocab, GPTQ_ERR_INVALID_ARG,
@@ -90,9 +96,10 @@ void check_logits(const void* logits, int dtype, int64_t rows, int32_t vocab, in
 }
 
 void check_teacher(int64_t rows, const float* t_values, const int32_t* t_indices,
-                   float temperature) {
+                   const float* weights, float temperature) {
   require(rows == 0 || (t_values != nullptr && t_indices != nullptr), GPTQ_ERR_INVALID_ARG,
           "distillation: null teacher values or indices");
+  check_words("distillation: misaligned teacher values, indices or weights", t_values, t_indices, weights);
   require(std::isfinite(temperature) && temperature > 0.0f && std::isfinite(1.0f / temperature) &&
               1.0f / temperature > 0.0f,
           GPTQ_ERR_INVALID_ARG, "distillation: temperature must be finite and > 0");
@@ -157,6 +164,7 @@ gptq_status gptq_fp8_quantize(const void* x, int xdtype, int64_t rows, int32_t c
     if (rows == 0 || cols == 0) return;
     require(x != nullptr && scales != nullptr && aligned(x, elt(xdtype)), GPTQ_ERR_INVALID_ARG,
             "gptq_fp8_quantize: null or misaligned x or scales");
+    check_words("gptq_fp8_quantize: misaligned scales", scales);
     const bool t = form == GPTQ_FP8_COLUMNS;
     check_codes(codes, ldc, t ? rows : cols, "gptq_fp8_quantize: null codes or too short rows",
                 "gptq_fp8_quantize: codes must be 16-byte aligned, ldc a multiple of 16");
@@ -318,6 +326,7 @@ gptq_status gptq_top_logits(const void* logits, int dtype, int64_t rows, int32_t
     require(k <= vocab, GPTQ_ERR_INVALID_ARG, "gptq_top_logits: k must be at most vocab");
     require(rows == 0 || (values != nullptr && indices != nullptr), GPTQ_ERR_INVALID_ARG,
             "gptq_top_logits: null values or indices");
+    check_words("gptq_top_logits: misaligned values, indices or lse", values, indices, lse);
     TopArgs a = {};
     a.logits = logits;
     a.ld = ld;
@@ -337,8 +346,9 @@ gptq_status gptq_distill_loss(const void* logits, int dtype, int64_t rows, int32
                               float* lse, void* stream) {
   return guarded([&] {
     check_logits(logits, dtype, rows, vocab, ld, k);
-    check_teacher(rows, t_values, t_indices, temperature);
+    check_teacher(rows, t_values, t_indices, weights, temperature);
     require(rows == 0 || loss != nullptr, GPTQ_ERR_INVALID_ARG, "gptq_distill_loss: null loss");
+    check_words("gptq_distill_loss: misaligned loss or lse", loss, lse);
     DistillArgs a = distill_args(logits, rows, vocab, ld, t_values, t_indices, k, temperature, weights);
     a.loss = loss;
     a.lse = lse;
@@ -354,8 +364,9 @@ gptq_status gptq_distill_backward(const void* logits, int dtype, int64_t rows, i
                                   int64_t ldd, void* stream) {
   return guarded([&] {
     check_logits(logits, dtype, rows, vocab, ld, k);
-    check_teacher(rows, t_values, t_indices, temperature);
+    check_teacher(rows, t_values, t_indices, weights, temperature);
     require(rows == 0 || lse != nullptr, GPTQ_ERR_INVALID_ARG, "gptq_distill_backward: null lse");
+    check_words("gptq_distill_backward: misaligned lse or grad_loss", lse, grad_loss);
     check_gradient(logits, dtype, rows, vocab, ld, dlogits, ldd);
     DistillArgs a = distill_args(logits, rows, vocab, ld, t_values, t_indices, k, temperature, weights);
     a.lse = const_cast<float*>(lse);
@@ -373,8 +384,9 @@ gptq_status gptq_distill_loss_grad(const void* logits, int dtype, int64_t rows, 
                                    float* loss, void* dlogits, int64_t ldd, void* stream) {
   return guarded([&] {
     check_logits(logits, dtype, rows, vocab, ld, k);
-    check_teacher(rows, t_values, t_indices, temperature);
+    check_teacher(rows, t_values, t_indices, weights, temperature);
     require(rows == 0 || loss != nullptr, GPTQ_ERR_INVALID_ARG, "gptq_distill_loss_grad: null loss");
+    check_words("gptq_distill_loss_grad: misaligned loss", loss);
     check_gradient(logits, dtype, rows, vocab, ld, dlogits, ldd);
     DistillArgs a = distill_args(logits, rows, vocab, ld, t_values, t_indices, k, temperature, weights);
     a.loss = loss;
