@@ -457,6 +457,16 @@ def _rows(t: torch.Tensor, name: str):
     return t.data_ptr(), n, m, ld
 
 
+def _one_device(t: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    """The library launches on the current device, with whatever addresses it is given."""
+    index = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != index:
+            raise ValueError(f"operands must be on one CUDA device, got {t.device} and {o.device}")
+    if index != torch.cuda.current_device():
+        raise ValueError(f"the operands' device, {t.device}, is not the current device")
+
+
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
     """An allocation in the order of the call's stream (the current one if none is given)."""
     if stream is None:
@@ -524,6 +534,7 @@ def gptq_fp8_quantize(x: torch.Tensor, form: str = "blocks", codes: Optional[tor
     if form not in FP8_FORMS:
         raise ValueError(f"form must be one of {sorted(FP8_FORMS)}")
     px, r, c, ldx = _rows(x, "x")
+    _one_device(x, codes, scales)
     given = codes, scales
     shape = (c, r) if form == "columns" else (r, c)
     sshape = {"rows": (_blocks(c), r), "columns": (_blocks(r), c),
@@ -548,6 +559,7 @@ def gptq_fp8_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     """y = x W^T for x [ntok, d_in] and a weight in 8-bit blocks (gptq_fp8_quantize); only
     enqueues."""
     px, t, k, ldx = _rows(x, "x")
+    _one_device(x, codes, scales, y, ws)
     pc, ldw, psc, n, d_in = _weight(codes, scales)
     if k != d_in:
         raise ValueError(f"x has {k} columns, the weight {d_in}")
@@ -578,6 +590,7 @@ def gptq_fp8_linear_backward(dy: torch.Tensor, x: Optional[torch.Tensor], codes:
     """(dx, dw) of y = x W^T from dy [ntok, d_out]; dx has dy's type, dw ``dw_dtype``; either
     is None where it is not asked for (x is needed for dw only).  Only enqueues."""
     pdy, t, n_dy, lddy = _rows(dy, "dy")
+    _one_device(dy, x, codes, scales, dx, dw, ws)
     pc, ldw, psc, n, k = _weight(codes, scales)
     if n_dy != n:
         raise ValueError(f"dy has {n_dy} columns, the weight {n} rows")
@@ -617,6 +630,7 @@ def gptq_top_logits(logits: torch.Tensor, k: int, values: Optional[torch.Tensor]
     indices int32 [rows, k], descending, equal values by ascending index, and the rows'
     log-sum-exp float32 [rows].  Only enqueues."""
     pl, n, v, ld = _rows(logits, "logits")
+    _one_device(logits, values, indices, lse)
     k, dev, given = int(k), logits.device, (values, indices, lse)
     if values is None:
         values = _empty((n, k), torch.float32, dev, stream)
@@ -651,6 +665,7 @@ def gptq_distill_loss(logits: torch.Tensor, values: torch.Tensor, indices: torch
     int32 [rows, k], -1 for no entry) to the student's softmax, and the log-sum-exp of the
     student's logits that gptq_distill_backward needs.  Only enqueues."""
     pl, n, v, ld = _rows(logits, "logits")
+    _one_device(logits, values, indices, weights, loss, lse)
     k, pv, pi, pw = _teacher(values, indices, weights, n)
     given = loss, lse
     if loss is None:
@@ -681,6 +696,7 @@ def gptq_distill_backward(logits: torch.Tensor, lse: torch.Tensor, values: torch
     """The gradient of gptq_distill_loss for the gradient ``grad_loss`` [rows] of its rows'
     losses; ``dlogits`` may be the logits themselves.  Only enqueues."""
     pl, n, v, ld = _rows(logits, "logits")
+    _one_device(logits, lse, values, indices, grad_loss, weights, dlogits)
     k, pv, pi, pw = _teacher(values, indices, weights, n)
     given = dlogits
     dlogits, pd, ldd = _gradient(logits, dlogits, stream)
@@ -700,6 +716,7 @@ def gptq_distill_loss_grad(logits: torch.Tensor, values: torch.Tensor, indices: 
     """(loss, dlogits) in one call: gptq_distill_loss, and the gradient of the losses' sum;
     ``dlogits`` may be the logits themselves.  Only enqueues."""
     pl, n, v, ld = _rows(logits, "logits")
+    _one_device(logits, values, indices, weights, loss, dlogits)
     k, pv, pi, pw = _teacher(values, indices, weights, n)
     given = loss, dlogits
     if loss is None:
