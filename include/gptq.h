@@ -438,9 +438,9 @@ gptq_status gptq_set_wait_limit(uint64_t limit_ns);
  *
  * A group of 128 values (the last of an axis may be shorter) with largest magnitude amax has
  *     scale = max(amax / 448, 2^-126)        code = e4m3(x / scale)
- * both quotients in float32 rounded to nearest, the code rounded to nearest even.  A group
- * that holds a NaN or an infinity gets a non-finite scale, and what is computed from it
- * comes out non-finite.
+ * both quotients in float32 rounded to nearest, the code rounded to nearest even; a code has
+ * its value's sign, also where it is zero.  A group that holds a NaN or an infinity gets a
+ * non-finite scale, and what is computed from it comes out non-finite.
  */
 typedef enum {
   GPTQ_FP8_ROWS = 1,     /* 1 x 128: codes [rows, cols], scales [ceil(cols/128), rows]       */

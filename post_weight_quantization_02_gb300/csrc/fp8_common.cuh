@@ -141,33 +141,40 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
 // one ulp of the quotient and q + (x - q s) y rounds it correctly (Markstein's theorem), as
 // long as nothing under- or overflows.  Scales outside [2^-80, 2^100] take the division itself;
 // y = 0 marks them.  In an all-zero group (padding, masked tokens) any y will do.
-__device__ __forceinline__ float reciprocal_of(uint32_t amax, float s) {
-  if (amax == 0) return 1.0f;
-  return s >= 0x1p-80f && s <= 0x1p100f ? __frcp_rn(s) : 0.0f;
+//
+// What is computed is -x / s, with -y in y's place, and the codes' signs are turned back (an
+// operation for four): for x = -0 the corrected quotient adds +0 to -0 and would lose the sign,
+// the negated one adds two zeros of the sign that it needs, for either x.
+__device__ __forceinline__ float minus_reciprocal_of(uint32_t amax, float s) {
+  if (amax == 0) return -1.0f;
+  return s >= 0x1p-80f && s <= 0x1p100f ? -__frcp_rn(s) : 0.0f;
 }
+constexpr uint32_t kTurnSigns = 0x80808080u;  // of four codes
 static __device__ __noinline__ float2 divide_pair(float2 x, float s) {
   return make_float2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s));
 }
-__device__ __forceinline__ float2 quotient(float2 x, float2 s, float2 y) {
+// -x / s, y as minus_reciprocal_of gives it
+__device__ __forceinline__ float2 minus_quotient(float2 x, float2 s, float2 y) {
   const float2 q = tc::mul2(x, y);
-  return tc::fma2(tc::fma2(q, make_float2(-s.x, -s.y), x), y, q);
+  return tc::fma2(tc::fma2(q, s, x), y, q);
 }
 __device__ __forceinline__ uint32_t codes2(float2 q) {
   return __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
 }
 
-// the codes of a thread's eight values of a row, all with scale s
+// the codes of a thread's eight values of a row, all with scale s (y: minus_reciprocal_of)
 template <typename T>
 __device__ __forceinline__ uint2 codes8(const Eight<T>& e, float s, float y) {
-  uint32_t c[4];
+  uint32_t c[4], turn = 0;
   if (y != 0.0f) {
+    turn = kTurnSigns;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = codes2(quotient(e.pair(j), make_float2(s, s), make_float2(y, y)));
+    for (int j = 0; j < 4; ++j) c[j] = codes2(minus_quotient(e.pair(j), make_float2(s, s), make_float2(y, y)));
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[j] = codes2(divide_pair(e.pair(j), s));
   }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  return make_uint2((c[0] | (c[1] << 16)) ^ turn, (c[2] | (c[3] << 16)) ^ turn);
 }
 
 }  // namespace gptq

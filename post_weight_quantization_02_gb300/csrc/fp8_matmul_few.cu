@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(THREADS + (std::is_void_v<TX> ? 0 : 32 * QUANT
             for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float s = scale_of(m);
             // the 128-byte swizzle: 16-byte pieces of a row exchanged by its number mod 8
-            const uint2 c = codes8(v[j], s, reciprocal_of(m, s));
+            const uint2 c = codes8(v[j], s, minus_reciprocal_of(m, s));
             if (i < nb) {
               uint8_t* dst = smem + i % NSTAGE * STAGE_BYTES + W_BYTES + token * BK;
               *reinterpret_cast<uint2*>(dst + (((c8 >> 1) ^ (token & 7)) << 4) + (c8 & 1) * 8) = c;

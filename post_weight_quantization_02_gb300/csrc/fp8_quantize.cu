@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantAr
   constexpr bool ROWS = (FORMS & GPTQ_FP8_ROWS) != 0, COLUMNS = (FORMS & GPTQ_FP8_COLUMNS) != 0,
                  BLOCKS = (FORMS & GPTQ_FP8_BLOCKS) != 0;
   __shared__ MaxPair<T> colmax[COLUMNS ? kThreads / 32 : 1][64];  // of each warp's 16 rows
-  __shared__ float2 colscale[COLUMNS ? 128 : 1];                  // scale, reciprocal
+  __shared__ float2 colscale[COLUMNS ? 128 : 1];                  // scale, minus its reciprocal
   __shared__ uint32_t warpmax[kThreads / 32];
   __shared__ uint2 tile[COLUMNS ? 128 * 16 : 1];  // [column][8-row chunk ^ c8]
 
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantAr
       }
     }
     m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
-    const float mine = scale_of(m[0]), inverse = reciprocal_of(m[0], mine);
+    const float mine = scale_of(m[0]), inverse = minus_reciprocal_of(m[0], mine);
     if ((c8 & 1) == 0 && c8 / 2 < nrow) a.scales[static_cast<int64_t>(ct) * a.lds + row0 + c8 / 2] = mine;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantAr
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) m = max(m, warpmax[w]);
-    const float s = scale_of(m), y = reciprocal_of(m, s);
+    const float s = scale_of(m), y = minus_reciprocal_of(m, s);
     if (tid == 0) a.scales[rt * a.col_tiles + ct] = s;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantAr
       for (int w = 1; w < kThreads / 32; ++w) p.join(colmax[w][tid / 2]);
       const uint32_t m = tid % 2 == 0 ? p.even() : p.odd();
       const float s = scale_of(m);
-      colscale[tid] = make_float2(s, reciprocal_of(m, s));
+      colscale[tid] = make_float2(s, minus_reciprocal_of(m, s));
       if (ct * 128 + tid < a.cols) a.scales_t[rt * a.lds_t + ct * 128 + tid] = s;
     }
     __syncthreads();
@@ -185,10 +185,11 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantAr
     for (int j = 0; j < 4; ++j) {
       const float2 se = colscale[8 * c8 + 2 * j], so = colscale[8 * c8 + 2 * j + 1];
       const float2 s = make_float2(se.x, so.x), y = make_float2(se.y, so.y);
-      uint32_t c[8];  // the even column's code in the low byte, the odd one's above
+      uint32_t c[8], turn = 0;  // the even column's code in the low byte, the odd one's above
       if (y.x != 0.0f && y.y != 0.0f) {
+        turn = kTurnSigns;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = codes2(quotient(v[i].pair(j), s, y));
+        for (int i = 0; i < 8; ++i) c[i] = codes2(minus_quotient(v[i].pair(j), s, y));
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -198,8 +199,8 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantAr
       }
       // a column's chunks of 8 rows are permuted by its c8, so that the 16 lanes that store
       // one row group hit 16 different bank pairs
-      const uint32_t a0 = __byte_perm(c[0], c[1], 0x5140), a1 = __byte_perm(c[2], c[3], 0x5140);
-      const uint32_t a2 = __byte_perm(c[4], c[5], 0x5140), a3 = __byte_perm(c[6], c[7], 0x5140);
+      const uint32_t a0 = __byte_perm(c[0], c[1], 0x5140) ^ turn, a1 = __byte_perm(c[2], c[3], 0x5140) ^ turn;
+      const uint32_t a2 = __byte_perm(c[4], c[5], 0x5140) ^ turn, a3 = __byte_perm(c[6], c[7], 0x5140) ^ turn;
       tile[(8 * c8 + 2 * j) * 16 + (rg ^ c8)] =
           make_uint2(__byte_perm(a0, a1, 0x5410), __byte_perm(a2, a3, 0x5410));
       tile[(8 * c8 + 2 * j + 1) * 16 + (rg ^ c8)] =

@@ -1,13 +1,40 @@
-"""The 8-bit products where a CTA works on many tiles and blocks."""
+"""The 8-bit quantiser's code bytes, and the products where a CTA works on many tiles and blocks."""
 
 import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_fp8 import (BF16, F32, check_product, dequantized, make_layer, np32,
-                                weight_values)
+from tests.test_gpu_fp8 import (BF16, E4M3, F32, check_product, dequantized, make_layer, np32,
+                                quantize_ref, weight_values)
 
 pytestmark = pytest.mark.gpu
+
+
+def code_bytes(values):
+    """Bytes of e4m3 values, the sign of zero included."""
+    return (np.searchsorted(E4M3, np.abs(values)) | (np.signbit(values) << 7)).astype(np.uint8)
+
+
+@pytest.mark.parametrize("form", ["rows", "columns", "blocks"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_quantize_bytes(lib, cuda_device, form, dtype):
+    """The codes are those of the division's quotient, byte for byte: zeros of either sign and
+    numbers that round to them keep their sign, at ordinary scales, extreme ones and in groups
+    that hold nothing else."""
+    rng = np.random.default_rng(41)
+    x = rng.standard_normal((520, 400)) * np.exp2(rng.integers(-14, 1, (520, 400)))
+    x[rng.random(x.shape) < 0.2] = -0.0
+    x[rng.random(x.shape) < 0.2] = 0.0
+    x[:128] *= 2.0 ** -100              # scales below 2^-80, where the division itself is taken
+    x[128:256] *= 2.0 ** 110            # and above 2^100
+    x[256:384, :128] = np.where(rng.random((128, 128)) < 0.5, -0.0, 0.0)
+    xt = torch.from_numpy(x.astype(np.float32)).to(dtype)
+    codes, scales = lib.gptq_fp8_quantize(xt.to(cuda_device), form)
+    ref, sref = quantize_ref(np32(xt), form)
+    assert np.array_equal(scales.cpu().numpy(), sref)
+    want = code_bytes(ref)
+    assert (want == 0x80).sum() > 10000
+    assert np.array_equal(codes.view(torch.uint8).cpu().numpy(), want)
 
 
 def varied(rng, r, c, dtype, dev):
