@@ -533,7 +533,9 @@ gptq_status gptq_top_logits(const void* logits, int dtype, int64_t rows, int32_t
  *     loss = w sum_j q_j (log q_j - s_{i_j} / T + Z)           (KL divergence, times w)
  *     dlogits_v = g w (exp(s_v / T - Z) - Q_v) / T,            Q_v = sum of the q_j at v
  * gptq_distill_loss writes loss and Z, gptq_distill_backward takes Z and the gradient g of
- * each row's loss, gptq_distill_loss_grad does both at once with g = 1.
+ * each row's loss, gptq_distill_loss_grad does both at once with g = 1.  Z is rounded to
+ * float32: where it is beyond 1024 either way gptq_distill_backward reads the row once more
+ * and sums it up again.
  *
  * logits     device [rows, vocab] of type dtype, rows ld elements apart, any alignment
  * t_values   device float32 [rows, k]; -inf is probability 0

@@ -322,10 +322,15 @@ __global__ void __launch_bounds__(S::kBlock, S::kPerSm) distill_kernel(const Dis
 
 // ------------------------------------------------------------------ the gradient alone
 
+// The log-sum-exp Z comes rounded to float32, and the rounding is a relative error of p.  Up to
+// this size it is at most 2^-15; rows beyond it (masked throughout by the type's lowest value, or far
+// from zero), whose Z may even be infinite, are summed up again.
+constexpr float kLseKept = 1024.0f;
+
 template <typename T, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) distill_backward_kernel(const DistillArgs a) {
   using V = LogitVec<T>;
-  __shared__ MaxSum tpairs[NT / 32];
+  __shared__ MaxSum tpairs[NT / 32], zpairs[NT / 32];
   __shared__ Entries<T> entries;
 
   const int64_t row = blockIdx.x;
@@ -350,13 +355,23 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_backward_kernel(const D
     entries.s[tid] = V::put(at_idx);
     entries.i[tid] = e.idx;
   }
-  // p = exp2((s / T - Z) log2 e); where no logit is above -inf, p is 0
+  // p = exp2((s / T - Z) log2 e), or exp2((s - m) c) / sum; where no logit is above -inf, p is 0
   const float g = w * a.inv_temp * (a.grad_loss != nullptr ? a.grad_loss[row] : 1.0f);
   const float lse = a.lse[row];
-  const float scale = lse == -INFINITY ? 0.0f : 1.0f;
-  const Gradient grad{a.inv_temp, base_of(lse), kLog2e, g * scale};
+  float scale = 1.0f;
+  Gradient grad{a.inv_temp, lse, kLog2e, g};
   const RowSpan<T> sp(x, 0, a.vocab);
   const uint4* xv = reinterpret_cast<const uint4*>(x + sp.head);
+  if (!(fabsf(lse) <= kLseKept)) {  // as the loss does; the row is read before any of it is written
+    MaxSum z = stream_pieces<T, NT>(xv, 0, sp.nvec, c);
+    const int edge = tid < sp.head ? tid : sp.tail0 + tid - sp.head;
+    if (tid < sp.head + (sp.end - sp.tail0)) z = join(z, max_sum_of(V::get(x[edge])), c);
+    leave_pair(z, c, zpairs);
+    __syncthreads();
+    z = take_pair<NT>(c, zpairs);
+    scale = z.m == -INFINITY ? 0.0f : 1.0f / z.s;
+    grad = Gradient{1.0f, base_of(z.m), c, g * scale};
+  }
   T* dv = dx + sp.head;
   const bool aligned16 = reinterpret_cast<uintptr_t>(dv) % 16 == 0;
   int p = tid;
