@@ -393,11 +393,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_backward_kernel(const D
                 [&](float v) { return scale * grad.exponential(v); });
 }
 
-template <typename T, typename S>
-void launch_ring(const DistillArgs& a, bool grad, cudaStream_t s) {
+template <typename T, typename S, bool GRAD>
+void launch_ring(const DistillArgs& a, cudaStream_t s) {
   const int64_t most = S::kPerSm * static_cast<int64_t>(sm_count());
   const unsigned grid = static_cast<unsigned>(a.rows < most ? a.rows : most);
-  auto kernel = grad ? distill_kernel<T, S, true> : distill_kernel<T, S, false>;
+  auto kernel = distill_kernel<T, S, GRAD>;
   ensure_dynamic_smem(kernel, S::kBytes);
   GPTQ_LAUNCH(GPTQ_K_DISTILL, s, kernel, grid, S::kBlock, S::kBytes, a);
 }
@@ -407,8 +407,9 @@ void launch_typed(const DistillArgs& a, bool loss, bool grad, cudaStream_t s) {
   if (loss) {
     // the loss alone reads a row once: two CTAs an SM whatever its length (2048 x 131072 bf16:
     // 86 us, 97 with one)
-    if (grad && !small_rows(static_cast<int64_t>(a.vocab) * sizeof(T))) launch_ring<T, LongRows<sizeof(T) == 2 ? 7 : 6>>(a, grad, s);
-    else launch_ring<T, ShortRows>(a, grad, s);
+    if (!grad) launch_ring<T, ShortRows, false>(a, s);
+    else if (small_rows(static_cast<int64_t>(a.vocab) * sizeof(T))) launch_ring<T, ShortRows, true>(a, s);
+    else launch_ring<T, LongRows<sizeof(T) == 2 ? 7 : 6>, true>(a, s);
     return;
   }
   const unsigned grid = static_cast<unsigned>(a.rows);

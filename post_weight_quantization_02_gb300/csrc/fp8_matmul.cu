@@ -40,8 +40,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <map>
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.cuh"
