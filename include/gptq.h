@@ -412,9 +412,10 @@ gptq_status gptq_check_wait_timeout(uint64_t limit_ns, void* ws, size_t ws_bytes
 
 /*
  * gptq_set_wait_limit -- the time limit of the tensor-core kernels' device waits (the
- * Hessian SYRK, the prepare's tf32x3 GEMMs, the lazy update, the 8-bit products), for every
- * later call in this process (all threads, all devices).  Not part of the method: a diagnostic that lets
- * a test make the kernels' pipeline waits run out on purpose.
+ * Hessian SYRK, the prepare's tf32x3 GEMMs, the lazy update, the 8-bit products) and of the
+ * distillation's, for every later call in this process (all threads, all devices).  Not part
+ * of the method: a diagnostic that lets a test make the kernels' pipeline waits run out on
+ * purpose.
  *
  * A pipeline wait (for a copy, a matrix operation or an accumulator) gives up after
  * limit_ns nanoseconds (2 s by default); the kernel then records GPTQ_ERR_TIMEOUT in the
@@ -544,8 +545,8 @@ gptq_status gptq_top_logits(const void* logits, int dtype, int64_t rows, int32_t
  * k          1 .. 256
  * temperature  finite, > 0
  * weights    device float32 [rows] (w), or null for 1.  A row of weight 0, or without an
- *            entry of non-zero q, does not count: its logits are not read, its loss, Z and
- *            gradient are 0
+ *            entry of non-zero q, does not count: its loss, Z and gradient are 0 whatever its
+ *            logits are, and those of a row of weight 0 are not read
  * loss, lse  device float32 [rows]; lse (Z) may be null in gptq_distill_loss
  * grad_loss  device float32 [rows] (g), or null for 1
  * dlogits    device [rows, vocab] of type dtype, rows ldd elements apart; may be logits

@@ -11,7 +11,7 @@
 // Bound by memory: a logit is read once from HBM and its gradient written once.  The loss
 // streams rows through a ring in shared memory (row_ring.cuh) and keeps a running maximum and
 // sum.  For the gradient the last chunks of the row are still in the ring; they are worked off
-// first, the others are fetched again behind them (from L2, where the rows in flight, two an
+// first, the others are fetched again behind them (from L2, where the long rows in flight, one an
 // SM, stay), so that the copies for this row's gradient and for the next row never wait for the
 // row's end.  The entries' columns are written once more with their q.
 #include <cuda_bf16.h>

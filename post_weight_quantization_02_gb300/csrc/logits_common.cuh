@@ -15,8 +15,9 @@ constexpr int kMaxTop = 256;
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Threads of a row: 256, four rows an SM, where a row is short and the latencies at its ends
-// count; else 512, two rows an SM, so that the rows in flight stay in L2 for their second pass.
+// Whether a row is short, so that the latencies at its ends count: it gets 256 threads, a long one
+// 512, and an SM about twice as many short rows at a time as long ones (top logits six and three,
+// gradient alone four and two, loss and gradient two and one).
 inline bool small_rows(int64_t row_bytes) { return row_bytes <= 96 * 1024; }
 
 template <typename T>
