@@ -1,10 +1,11 @@
-"""The distillation loss on rows whose logits are far from zero."""
+"""The top logits and the distillation loss on many rows (a CTA works on several), and on rows whose
+logits are far from zero."""
 
 import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_distill import BF16, F32, make
+from tests.test_gpu_distill import BF16, F32, INF, NAN, check_top, make
 
 pytestmark = pytest.mark.gpu
 
@@ -39,6 +40,34 @@ def check(loss, grad, ref, size, w, g, temp, dtype, extra=0.0):
     err = np.abs(grad.double().cpu().numpy() - rg)
     tol = (np.abs(g * w) / temp)[:, None] * ((rel + extra) * (p + Q))
     assert np.all(err <= tol + (2.0 ** -8 * np.abs(rg) if dtype == BF16 else 0) + 1e-37)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n,v", [(1000, 3001), (700, 60001)])   # short rows and long ones
+def test_distill_many_rows(lib, cuda_device, dtype, n, v):
+    """Several rows a CTA, some of weight 0 (whose logits are not read) and some without entries
+    among them: loss alone, loss and gradient, the two calls, and in place."""
+    gen = torch.Generator().manual_seed(n)
+    x, tv, ti, w, gl = make(gen, n, v, 24, dtype, cuda_device)
+    w[torch.rand(n, generator=gen).to(cuda_device) < 0.3] = 0.0
+    ti[torch.rand(n, generator=gen).to(cuda_device) < 0.2] = -1
+    ti[5::7, 3] = ti[5::7, 0]
+    hw, hg = w.double().cpu().numpy(), gl.double().cpu().numpy()
+    ref = reference(x, tv, ti, 2.0, hw, np.ones(n))
+    x[w == 0] = NAN
+    size = 40.0
+    loss, lse = lib.gptq_distill_loss(x, tv, ti, temperature=2.0, weights=w)
+    dx = lib.gptq_distill_backward(x, lse, tv, ti, gl, temperature=2.0, weights=w)
+    check(loss, dx, (ref[0], ref[1] * hg[:, None], *ref[2:]), size, hw, hg, 2.0, dtype)
+    loss2, dx2 = lib.gptq_distill_loss_grad(x, tv, ti, temperature=2.0, weights=w)
+    check(loss2, dx2, ref, size, hw, np.ones(n), 2.0, dtype)
+    same = x.clone()
+    loss3, dx3 = lib.gptq_distill_loss_grad(same, tv, ti, temperature=2.0, weights=w, dlogits=same)
+    assert torch.equal(loss3, loss2) and torch.equal(dx3, dx2)
+    same = x.clone()
+    dx4 = lib.gptq_distill_backward(same, lse, tv, ti, gl, temperature=2.0, weights=w, dlogits=same)
+    assert torch.equal(dx4, dx)
+    lib.gptq_async_status()
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -83,3 +112,13 @@ def test_distill_backward_far_from_zero(lib, cuda_device, dtype, temp):
     out = lib.gptq_distill_backward(same, lse, tv, ti, gl, temperature=temp, weights=w, dlogits=same)
     assert torch.equal(out, dx)
     lib.gptq_async_status()
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(400, 2000, BF16), (50, 1003, F32), (3, 1500, BF16)])
+def test_top_logits_of_few_pieces(lib, cuda_device, rows, vocab, dtype):
+    """Fewer 16-byte pieces in a row than k, so that most threads see no element, and more elements
+    than are held as candidates."""
+    gen = torch.Generator().manual_seed(vocab)
+    x = (torch.randn(rows, vocab, generator=gen) * 3).to(dtype).to(cuda_device)
+    x[1, 5:900] = -INF
+    check_top(lib, x, 256)

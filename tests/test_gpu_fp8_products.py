@@ -37,6 +37,46 @@ def test_quantize_bytes(lib, cuda_device, form, dtype):
     assert np.array_equal(codes.view(torch.uint8).cpu().numpy(), want)
 
 
+def test_linear_gradients_are_exact_differences(lib, cuda_device):
+    """On inputs that the quantisers represent exactly, an entry of x moves one token's outputs
+    and an entry of W one column of them, and the gradients are those differences, weighted by dy.
+    Both sides are within check_product's bound, 128 2^-23 + 3 blocks 2^-24 of the terms'
+    magnitudes, which at the entries taken is under 5 % of the gradient."""
+    rng = np.random.default_rng(11)
+    t, n, k = 6, 130, 260
+    grid = E4M3[(E4M3 >= 1) & (E4M3 <= 448)]
+    def exact_grid(r, c):
+        m = rng.choice(grid, (r, c)) * rng.choice([-1.0, 1.0], (r, c))
+        # every group (1 x 128 either way, 128 x 128) reaches 448, so that its scale is 1
+        m[np.arange(r) % 128 == 0, :] = 448
+        m[:, np.arange(c) % 128 == 0] = 448
+        return m
+    x, w, dy = exact_grid(t, k), exact_grid(n, k), exact_grid(t, n)
+    points = [(1, 1), (5, 259), (3, 130), (2, 77), (4, 200)]
+    for i, j in points:
+        x[i, j] = w[i, j] = 448 if (i + j) % 2 else -416
+    dev = lambda a: torch.from_numpy(a.astype(np.float32)).to(cuda_device)
+    gamma = lambda m: 128 * 2.0 ** -23 + 3 * -(-m // 128) * 2.0 ** -24
+    def outputs():
+        y = lib.gptq_fp8_linear(dev(x), *lib.gptq_fp8_quantize(dev(w)), dtype=F32)
+        return y.double().cpu().numpy(), gamma(k) * (np.abs(x) @ np.abs(w).T)
+    codes, scales = lib.gptq_fp8_quantize(dev(w))
+    dx, dw = lib.gptq_fp8_linear_backward(dev(dy), dev(x), codes, scales)
+    base, tol = outputs()
+    bx, bw = gamma(n) * (np.abs(dy) @ np.abs(w)), gamma(t) * (np.abs(dy).T @ np.abs(x))
+    for i, j in points:
+        for m, grad, own, part in ((x, dx, bx, np.s_[i, :]), (w, dw, bw, np.s_[:, i])):
+            old = m[i, j]
+            m[i, j] = -old
+            moved = outputs()[0]
+            m[i, j] = old
+            diff = ((moved - base)[part] * dy[part]).sum() / (-2 * old)
+            bound = 2 * (tol[part] * np.abs(dy[part])).sum() / (2 * abs(old)) + own[i, j]
+            got = float(grad[i, j])
+            assert bound <= 0.05 * abs(diff), (bound, diff)
+            assert abs(diff - got) <= bound, (diff, got, bound)
+
+
 def varied(rng, r, c, dtype, dev):
     """Values whose groups of 128, along either axis, differ in size by powers of two."""
     x = rng.standard_normal((r, c))
@@ -85,4 +125,18 @@ def test_products_with_scales_of_every_size(lib, cuda_device, t, n, k):
     for _ in range(5):
         assert torch.equal(lib.gptq_fp8_linear(x, codes, scales, dtype=F32), y)
         assert torch.equal(back(), dx)
+    lib.gptq_async_status()
+
+
+def test_gradients_of_a_long_vocabulary(lib, cuda_device):
+    """An output head: the input gradient contracts over 131072 entries, the weight gradient has as
+    many rows."""
+    t, n, k = 300, 131072, 256
+    g = torch.Generator().manual_seed(47)
+    codes, scales = make_layer(lib, g, n, k, cuda_device)
+    rng = np.random.default_rng(47)
+    x, dy = varied(rng, t, k, BF16, cuda_device), varied(rng, t, n, BF16, cuda_device)
+    dx, dw = lib.gptq_fp8_linear_backward(dy.float(), x, codes, scales)
+    check_product(dx, dequantized(np32(dy), "rows"), weight_values(codes, scales))
+    check_product(dw, dequantized(np32(dy), "columns").T, dequantized(np32(x), "columns"))
     lib.gptq_async_status()
