@@ -457,8 +457,16 @@ def _rows(t: torch.Tensor, name: str):
     return t.data_ptr(), n, m, ld
 
 
+@functools.lru_cache(maxsize=1)
+def _devices() -> int:
+    return torch.cuda.device_count()
+
+
 def _one_device(t: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
-    """The library launches on the current device, with whatever addresses it is given."""
+    """The library launches on the current device, with whatever addresses it is given.  (Where
+    there is one device, CUDA tensors are on it: a microsecond less a call.)"""
+    if _devices() == 1:
+        return
     index = t.get_device()
     for o in others:
         if o is not None and o.get_device() != index:
@@ -578,7 +586,8 @@ def gptq_fp8_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     _check(lib().gptq_fp8_linear(px, _dtype_code(x), t, ldx, pc, ldw, psc, n, k, py,
                                  _dtype_code(y), ldy, _ptr(ws), 0 if ws is None else ws.numel(),
                                  _stream_of(stream, x)))
-    _wrote(given)
+    if given is not None:
+        _wrote(given)
     return y
 
 
@@ -705,7 +714,8 @@ def gptq_distill_backward(logits: torch.Tensor, lse: torch.Tensor, values: torch
                                        float(temperature), pw,
                                        _buf(grad_loss, torch.float32, n, "grad_loss"), pd, ldd,
                                        _stream_of(stream, logits)))
-    _wrote(given)
+    if given is not None:
+        _wrote(given)
     return dlogits
 
 

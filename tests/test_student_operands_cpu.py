@@ -90,6 +90,7 @@ def fake(monkeypatch):
     monkeypatch.setattr(G, "lib", lambda: recorder)
     monkeypatch.setattr(G, "_stream_of", lambda stream, t: 0)
     monkeypatch.setattr(torch.autograd.graph, "increment_version", lambda t: None)
+    monkeypatch.setattr(G, "_devices", lambda: 2)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     return recorder
 
