@@ -100,8 +100,8 @@ void check_teacher(int64_t rows, const float* t_values, const int32_t* t_indices
   require(rows == 0 || (t_values != nullptr && t_indices != nullptr), GPTQ_ERR_INVALID_ARG,
           "distillation: null teacher values or indices");
   check_words("distillation: misaligned teacher values, indices or weights", t_values, t_indices, weights);
-  require(std::isfinite(temperature) && temperature > 0.0f && std::isfinite(1.0f / temperature) &&
-              1.0f / temperature > 0.0f,
+  // the kernels work with log2(e) / T
+  require(std::isfinite(temperature) && temperature > 0.0f && std::isfinite(kLog2e / temperature),
           GPTQ_ERR_INVALID_ARG, "distillation: temperature must be finite and > 0");
 }
 

@@ -24,6 +24,14 @@ def test_misaligned_pointers(name, defaults, fields):
             assert "aligned" in G.gptq_last_error()
 
 
+@pytest.mark.parametrize("name,defaults", [("gptq_distill_loss", LOSS), ("gptq_distill_backward", GRAD),
+                                           ("gptq_distill_loss_grad", BOTH)])
+def test_temperature_whose_exponent_factor_overflows(name, defaults):
+    """log2(e) / T has to be a finite float32 number: 4.8e38, of T = 3e-39, is not, 3.2e38 is."""
+    assert call(name, defaults, dict(T=3e-39)) == INVALID
+    assert call(name, defaults, dict(T=4.5e-39, rows=0)) != INVALID     # (no GPU: no status word)
+
+
 class Operand:
     """What the binding looks at in a CUDA tensor."""
 
