@@ -324,7 +324,8 @@ __global__ void __launch_bounds__(S::kBlock, S::kPerSm) distill_kernel(const Dis
 
 // The log-sum-exp Z comes rounded to float32, and the rounding is a relative error of p.  Up to
 // this size it is at most 2^-15; rows beyond it (masked throughout by the type's lowest value, or far
-// from zero), whose Z may even be infinite, are summed up again.
+// from zero), whose Z may even be infinite, are summed up again (2048 x 131072 bf16 165 us, 215 where
+// all rows are).
 constexpr float kLseKept = 1024.0f;
 
 template <typename T, int NT>

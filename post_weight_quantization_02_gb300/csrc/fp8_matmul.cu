@@ -18,14 +18,16 @@
 //   warp 1      TMEM owner (every CTA); in the even CTA the MMA issuer
 //   warp 2      sees a block's scales land in this CTA and passes that on to the epilogue (every
 //               CTA): a completed MMA says that copies have landed, but makes what they wrote
-//               visible to no thread (the epilogue's own wait for the scales cost 7 %)
+//               visible to no thread (a wait of the epilogue's own for them cost about 7 %)
 //   warps 4..11 epilogue (every CTA): thread = one row of C, 128 columns in registers (or 4 rows,
 //               32 columns: below)
 // Two 256-column accumulators alternate, so the MMAs of one block overlap the scaling of the
 // block before.  A block takes 700 to 800 cycles at 8192 x 8192 x 28672, 512 of them MMAs (1.37 ms,
 // 2.8 PFLOP/s).  Neither a multicast B over two pairs (1.44 ms), nor halves of 128 columns with a
 // completion and a hand-back of their own (1.45 ms), nor 16 epilogue warps of 64 columns (1.50 ms)
-// bring it nearer; TMEM has no room for a third accumulator of 256 columns.
+// bring it nearer; TMEM has no room for a third accumulator of 256 columns.  At a tile's end the sums
+// are stored while the tensor cores wait: 4 us a tile, 5.5 with column scales (4864 x 4096 results
+// over contractions of 1024 to 8192).
 //
 // Where the last wave of tiles, or the only one, leaves half of the pairs idle, a cluster of 2 or 4
 // pairs shares a tile of it (a launch of its own after the full waves): each pair takes

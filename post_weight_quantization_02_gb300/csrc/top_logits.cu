@@ -7,7 +7,9 @@
 // and few more do, all of them in the quarters whose maximum reaches it: only those (about 70 of
 // 2048 for k = 64) are read again, from L2, by whole warps, and the elements that reach the bound
 // are ranked by counting.  Where too many reach it (long runs of equal values), it is refined to
-// the exact k-th element by a radix selection over (key, index) pairs, which are all distinct.
+// the exact k-th element by a radix selection over (key, index) pairs, which are all distinct.  (So
+// it is in a row of fewer pieces than k, which has no bound, and more than 1024 elements: top 256 of
+// 2048 x 2000 bf16 255 us, top 128 of them 61.)
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -3,8 +3,9 @@
 ``Fp8Linear`` keeps a weight as e4m3 codes in 128 x 128 blocks (``gptq_fp8_quantize``) and
 multiplies activations, quantised in 1 x 128 groups on the way in, on the tensor cores
 (``gptq_fp8_linear``).  It can be made from a dense weight or from a packed GPTQ checkpoint
-(``QuantizedLayer``), and it is differentiable: the gradients of its input and of its weight
-are 8-bit products too (``gptq_fp8_linear_backward``; the quantisers count as the identity).
+(``QuantizedLayer``), and it is differentiable once, in reverse mode: the gradients of its input
+and of its weight are 8-bit products too (``gptq_fp8_linear_backward``; the quantisers count as the
+identity).
 Every call only enqueues; ``gptq.gptq_async_status`` reports device-side failures.
 """
 
